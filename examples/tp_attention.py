@@ -140,7 +140,9 @@ def run(ranks=2, hidden=4096, heads_q=32, heads_kv=8, head_dim=128, prompts=(204
             began = time.perf_counter()
             partials = [m.step(ctx, x.to(BF16), batch) for m in members]
             y = torch.empty_like(x)
-            ar.ar_reduce_add(ctx, [y], partials, y.numel(), ar.AR_F32, ar.AR_BF16, ar.AR_MODE_AUTO | ar.AR_SRC_WIRE, x)
+            # (the reduce takes its stream; the layer's operators are on torch's current one)
+            ar.ar_reduce_add(ctx, [y], partials, y.numel(), ar.AR_F32, ar.AR_BF16, ar.AR_MODE_AUTO | ar.AR_SRC_WIRE, x,
+                             stream=torch.cuda.current_stream())
             torch.cuda.synchronize()
             took = time.perf_counter() - began
             line = f"{'prompt' if step == 0 else 'token '} {sum(new):6d} rows, caches {max(lens)}: {took * 1e3:8.3f} ms"

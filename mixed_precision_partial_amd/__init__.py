@@ -24,7 +24,7 @@ The functions carry the C names:
 ready-made ``ptr_array(...)`` arrays (passed through unchanged, which keeps
 the per-call marshalling cost low for latency-bound callers); ``stream`` is a
 ``torch.cuda.Stream``, a raw ``hipStream_t`` integer, or None for the null
-stream.
+stream (for the layer operators torch's current stream).
 
 The library sees only pointers, so it cannot tell how large a buffer is.  With
 ``validate=True`` (the default) the enqueueing calls check, before calling it,
@@ -36,7 +36,8 @@ when they bind.
 
 The layer operators (``ar_qk_norm_rope`` to ``ar_fp8_matmul``) take torch tensors
 only: types, sizes and strides come from them, and a tensor that does not fit
-raises ``ValueError`` before the call.
+raises ``ValueError`` before the call.  Without a ``stream`` they are enqueued, as
+torch's own operations are, on torch's current stream of the tensors' device.
 """
 from __future__ import annotations
 
@@ -559,15 +560,25 @@ def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
-def _workspace(need: int, given, like, stream):
+def _call_stream(stream, like) -> int | None:
+    """The handle of a layer operator's stream: torch's current one unless another is given.  (Its
+    handle is asked for without making a stream object of it, which takes 2 of a single token's 10 us.)"""
+    if stream is not None or not like.is_cuda:
+        return _stream_handle(stream)
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
+
+
+def _workspace(need: int, given, like, stream, handle):
     """``given``, or bytes from torch's allocator for the stream of the call (so that
     they are not handed out again before the call's work there is done)."""
     if given is not None or need == 0:
         return given
     import torch
 
-    handle = _stream_handle(stream) or 0
-    if torch.cuda.current_stream(like.device).cuda_stream == handle:
+    handle = handle or 0
+    if stream is None or torch.cuda.current_stream(like.device).cuda_stream == handle:
         return torch.empty(need, dtype=torch.uint8, device=like.device)
     on = torch.cuda.ExternalStream(handle, like.device) if handle else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(on):
@@ -631,7 +642,7 @@ def ar_qk_norm_rope(ctx, q, k, q_weight=None, k_weight=None, table=None, positio
     shape, code = _layout("qk", tensors, (eps, interleaved), make)
     rc = lib.ar_qk_norm_rope(ctx, shape, code, q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out), q.data_ptr(), k.data_ptr(),
                              _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(table),
-                             None if table is None else positions.data_ptr(), _ptr(slots), _stream_handle(stream))
+                             None if table is None else positions.data_ptr(), _ptr(slots), _call_stream(stream, q))
     return _status(rc, "ar_qk_norm_rope", check, tensors)
 
 
@@ -690,10 +701,11 @@ def ar_attention(ctx, out, q, k, v, cu_q, k_start, k_len, max_q: int, max_k: int
     need = ctypes.c_size_t()
     rc = lib.ar_attention_workspace(ctypes.byref(s), code, ctypes.byref(need))
     if rc == AR_OK:
-        ws = _workspace(need.value, workspace, q, stream)
+        handle = _call_stream(stream, q)
+        ws = _workspace(need.value, workspace, q, stream, handle)
         rc = lib.ar_attention(ctx, ctypes.byref(s), code, out.data_ptr(), _ptr(lse), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                               cu_q.data_ptr(), k_start.data_ptr(), k_len.data_ptr(), _ptr(ws),
-                              0 if ws is None else ws.nbytes, _stream_handle(stream))
+                              0 if ws is None else ws.nbytes, handle)
     return _status(rc, "ar_attention", check, tensors)
 
 
@@ -722,7 +734,7 @@ def ar_fp8_quantize(ctx, codes, scales, x, stream=None, check: bool = True) -> i
         return rows, cols, _row(x, 8), codes_row, _type_code(x, "x")
     tensors = (codes, scales, x)
     sizes = _layout("quant", tensors, None, make)
-    rc = lib.ar_fp8_quantize(ctx, codes.data_ptr(), scales.data_ptr(), x.data_ptr(), *sizes, _stream_handle(stream))
+    rc = lib.ar_fp8_quantize(ctx, codes.data_ptr(), scales.data_ptr(), x.data_ptr(), *sizes, _call_stream(stream, x))
     return _status(rc, "ar_fp8_quantize", check, tensors)
 
 
@@ -760,9 +772,10 @@ def ar_fp8_matmul(ctx, out, a, a_scales, b, b_scales, workspace=None, stream=Non
     tensors = (out, a, a_scales, b, b_scales)
     shape, code, need, rc = _layout("mm", tensors, None, make)
     if rc == AR_OK:
-        ws = _workspace(need, workspace, out, stream)
+        handle = _call_stream(stream, out)
+        ws = _workspace(need, workspace, out, stream, handle)
         rc = lib.ar_fp8_matmul(ctx, shape, code, out.data_ptr(), a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
-                               b_scales.data_ptr(), _ptr(ws), 0 if ws is None else ws.nbytes, _stream_handle(stream))
+                               b_scales.data_ptr(), _ptr(ws), 0 if ws is None else ws.nbytes, handle)
     return _status(rc, "ar_fp8_matmul", check, tensors)
 
 

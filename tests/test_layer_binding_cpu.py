@@ -1,0 +1,54 @@
+"""What the binding of the layer operators hands to the library, seen by a stand-in for it, without a GPU."""
+from __future__ import annotations
+
+
+import pytest
+import torch
+
+import mixed_precision_partial_amd as ar
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is on a GPU."""
+    is_cuda = True
+
+
+def on_device(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice)
+
+
+class Recorder:
+    """Stands for the library: records the last argument of each call, its stream."""
+
+    def __init__(self):
+        self.streams = {}
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.streams[name] = args[-1]
+            return ar.AR_OK
+        return call
+
+
+def layer_calls(stream):
+    q, k, table, pos = on_device(4, 2, 64), on_device(4, 1, 64), on_device(9, 64, dtype=torch.float32), on_device(4, dtype=torch.int64)
+    ar.ar_qk_norm_rope(None, q, k, None, None, table, pos, stream=stream)
+    ar.ar_attention(None, torch.empty_like(q), q, k, k, on_device(2, dtype=torch.int32), on_device(1, dtype=torch.int64),
+                    on_device(1, dtype=torch.int32), 4, 4, stream=stream)
+    codes, scales = on_device(4, 128, dtype=torch.uint8), on_device(4, 1, dtype=torch.float32)
+    ar.ar_fp8_quantize(None, codes, scales, q.view(4, 128), stream=stream)
+    ar.ar_fp8_matmul(None, on_device(4, 4, dtype=torch.float32), codes, scales, codes, on_device(1, 1, dtype=torch.float32),
+                     stream=stream)
+
+
+@pytest.mark.parametrize("given", [None, 0, 0x7000])
+def test_calls_without_a_stream_go_to_the_current_one(monkeypatch, given):
+    """torch's current stream of the tensors' device unless a stream is given; 0 is the null stream."""
+    current = 0x5000
+    seen = Recorder()
+    monkeypatch.setattr(ar, "load_library", lambda: seen)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: current)
+    layer_calls(given)
+    want = current if given is None else given
+    for name in ("ar_qk_norm_rope", "ar_attention", "ar_fp8_quantize", "ar_fp8_matmul"):
+        assert seen.streams[name] == want, name
