@@ -660,7 +660,8 @@ def _attn_layout(out, q, k, v) -> ArAttn:
 
 def _attn_call(s: ArAttn, batch: int, max_q: int, max_k: int, causal: bool, scale) -> ArAttn:
     s = ArAttn.from_buffer_copy(s)
-    s.batch, s.max_q, s.max_k = batch, int(max_q), int(max_k)
+    # (an assignment to a C int drops what does not fit into it)
+    s.batch, s.max_q, s.max_k = batch, *(max(-1, min(int(x), (1 << 31) - 1)) for x in (max_q, max_k))
     s.scale = s.head_dim ** -0.5 if scale is None else float(scale)
     s.flags = AR_ATTN_CAUSAL if causal else 0
     return s

@@ -52,3 +52,24 @@ def test_calls_without_a_stream_go_to_the_current_one(monkeypatch, given):
     want = current if given is None else given
     for name in ("ar_qk_norm_rope", "ar_attention", "ar_fp8_quantize", "ar_fp8_matmul"):
         assert seen.streams[name] == want, name
+
+
+def attention_shapes(tokens, rows, heads_q=16, heads_kv=2, dim=128):
+    """out, q, k, v of a call by their sizes alone."""
+    q = torch.empty(tokens, heads_q, dim, dtype=torch.bfloat16, device="meta")
+    k = torch.empty(rows, heads_kv, dim, dtype=torch.bfloat16, device="meta")
+    return q, q, k, k
+
+
+@pytest.mark.parametrize("bound", [(1 << 31) - 1, 1 << 31, 1 << 32, (1 << 32) + 5, 1 << 70])
+def test_bounds_of_keys_past_32_bits_hold(bound):
+    """Any bound of the lengths holds that is not below them; a larger one is no smaller for the library."""
+    need = ar.ar_attention_workspace(*attention_shapes(1, 131072), 1, 1, 131072)
+    assert need > 0
+    assert ar.ar_attention_workspace(*attention_shapes(1, 131072), 1, 1, bound) == need
+
+
+@pytest.mark.parametrize("bounds", [(-1, 4), (4, -1), (-(1 << 32), 4), (4, -(1 << 32) + 3), (1 << 32, 4)], ids=str)
+def test_bounds_outside_the_limits_are_refused(bounds):
+    with pytest.raises(ar.ArError):
+        ar.ar_attention_workspace(*attention_shapes(4, 100), 1, *bounds)
