@@ -573,7 +573,10 @@ def _call_stream(stream, like) -> int | None:
 def _workspace(need: int, given, like, stream, handle):
     """``given``, or bytes from torch's allocator for the stream of the call (so that
     they are not handed out again before the call's work there is done)."""
-    if given is not None or need == 0:
+    if need == 0:
+        return None
+    if given is not None:
+        _need(given.is_contiguous(), "workspace: expected contiguous bytes")
         return given
     import torch
 

@@ -47,6 +47,7 @@ def test_calls_without_a_stream_go_to_the_current_one(monkeypatch, given):
     current = 0x5000
     seen = Recorder()
     monkeypatch.setattr(ar, "load_library", lambda: seen)
+    monkeypatch.setattr(ar, "_layouts", {})     # the stand-in's answers are not kept
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: current)
     layer_calls(given)
     want = current if given is None else given
@@ -73,3 +74,26 @@ def test_bounds_of_keys_past_32_bits_hold(bound):
 def test_bounds_outside_the_limits_are_refused(bounds):
     with pytest.raises(ar.ArError):
         ar.ar_attention_workspace(*attention_shapes(4, 100), 1, *bounds)
+
+
+@pytest.mark.parametrize("make", [lambda n: torch.zeros(2 * n, dtype=torch.uint8)[::2], lambda n: torch.zeros(n, 2, dtype=torch.uint8)[:, :1],
+                                  lambda n: torch.zeros(1, dtype=torch.uint8).expand(n)], ids=["every second", "a column", "expanded"])
+def test_workspaces_with_gaps_are_refused(monkeypatch, make):
+    """A call writes the bytes that follow the workspace's first: they have to be the workspace's own."""
+    class Needs(Recorder):
+        def __getattr__(self, name):
+            def call(*args):
+                if name.endswith("_workspace"):
+                    args[-1]._obj.value = 4096
+                    return ar.AR_OK
+                raise AssertionError(f"{name} was called")
+            return call
+    monkeypatch.setattr(ar, "load_library", Needs)
+    monkeypatch.setattr(ar, "_layouts", {})     # the stand-in's answers are not kept
+    q, k = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, 1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="workspace"):
+        ar.ar_attention(None, torch.empty_like(q), q, k, k, torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int64),
+                        torch.zeros(1, dtype=torch.int32), 4, 4, workspace=make(4096))
+    codes = torch.zeros(4, 128, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        ar.ar_fp8_matmul(None, torch.zeros(4, 4), codes, torch.zeros(4, 1), codes, torch.zeros(1, 1), workspace=make(4096))
