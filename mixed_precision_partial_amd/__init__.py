@@ -533,9 +533,7 @@ def _heads(x, what: str, like=None):
     if like is not None:
         _need(x.dtype == like.dtype and x.shape[2] == like.shape[2], f"{what}: type or head_dim differs from q's")
     dim = x.shape[2]
-    head = x.stride(1) if x.shape[1] > 1 else dim
-    token = x.stride(0) if x.shape[0] > 1 else max(dim, head * (x.shape[1] - 1) + dim)
-    return token, head
+    return x.stride(0) if x.shape[0] > 1 else dim, x.stride(1) if x.shape[1] > 1 else dim
 
 
 def _index(x, n: int, dtype: str, what: str) -> None:

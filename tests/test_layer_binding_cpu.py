@@ -97,3 +97,12 @@ def test_workspaces_with_gaps_are_refused(monkeypatch, make):
     codes = torch.zeros(4, 128, dtype=torch.uint8)
     with pytest.raises(ValueError, match="workspace"):
         ar.ar_fp8_matmul(None, torch.zeros(4, 4), codes, torch.zeros(4, 1), codes, torch.zeros(1, 1), workspace=make(4096))
+
+
+def test_single_rows_of_head_major_buffers():
+    """The one token of a [heads, tokens, head_dim] buffer: a single row's distance to the next is no limit."""
+    q = torch.empty(32, 8192, 128, dtype=torch.bfloat16, device="meta")[:, 5:6].transpose(0, 1)
+    k = torch.empty(8, 1 << 20, 128, dtype=torch.bfloat16, device="meta").transpose(0, 1)
+    assert ar.ar_attention_workspace(q, q, k, k, 1, 1, 131072) > 0
+    one = k[7:8]
+    assert ar.ar_attention_workspace(q, q, one, one, 1, 1, 1) == 0
