@@ -36,6 +36,12 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // many powers of two: until then the probabilities stay below 2^8, in range for every
 // type and no less exact.
 constexpr float kSlack = 8.0f;
+// Probabilities meet the values in the type, whose range is binary16's least: taken 2^7 times
+// as large, at most 2^15 with the slack, they keep what lies down to 2^-32 of the reference (without,
+// to 2^-25: 30000 keys at 2^-26 of one other's probability were lost altogether).  The sums of
+// a row have the factor too; it is a part of the reference that goes with them.
+template <int T>
+constexpr float kLift = T == AR_F16 ? 7.0f : 0.0f;
 
 template <int T>
 struct Mat;
@@ -278,7 +284,7 @@ LAYER_DEV float tile_top(const v16f (&s)[KT / 32]) {
 // Probabilities p up to the rows' references, and their sums.
 template <int T, int DB, int KT>
 LAYER_DEV void tile_powers(const v16f (&s)[KT / 32], float c, Rows<T, DB> &w, typename Mat<T>::frag (&p)[KT / 16]) {
-    const float mc = w.m == kNone ? 0.0f : w.m * c;
+    const float mc = (w.m == kNone ? 0.0f : w.m * c) - kLift<T>;
     float sum = 0.0f;
 #pragma unroll
     for (int t = 0; t < KT / 32; ++t) {
@@ -364,7 +370,7 @@ LAYER_DEV void tile_both(const char *vs, v16f (&s)[KT / 32], float c, Rows<T, DB
     typename Mat<T>::frag v[2][kFrags];
 #pragma unroll
     for (int i = 0; i < kFrags; ++i) v[0][i] = value_fragment<T, DB>(vs, i, 0);
-    const float mc = w.m == kNone ? 0.0f : w.m * c;
+    const float mc = (w.m == kNone ? 0.0f : w.m * c) - kLift<T>;
     float sum = 0.0f;
 #pragma unroll
     for (int h = 0; h < KT / 16; ++h) {
@@ -612,7 +618,7 @@ __global__ void __launch_bounds__(256 * S, DB <= 128 ? 2 / S : 1) k_attn_rows(At
     }
 
     float l = sum_halves(w.l);
-    float mc = w.m == kNone ? kNone : w.m * a.scale_log2;
+    float mc = w.m == kNone ? kNone : w.m * a.scale_log2 - kLift<T>;
     if constexpr (S == 2) {   // the second stream's lanes hand theirs to the first's, lane by lane
         v4f *const sums = reinterpret_cast<v4f *>(ks);
         float *const stats = reinterpret_cast<float *>(vs);
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(64 * W, DB <= 128 ? 2 : 1) k_attn_keys(AttnArg
     }
 
     // join the waves: each scales its sums to the common reference
-    const float mc_own = w.m == kNone ? kNone : w.m * a.scale_log2;
+    const float mc_own = w.m == kNone ? kNone : w.m * a.scale_log2 - kLift<T>;
     const float l_own = sum_halves(w.l);
     if (lane < 32) {
         stat[wave][0][lane] = mc_own;
