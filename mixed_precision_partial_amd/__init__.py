@@ -38,6 +38,8 @@ The layer operators (``ar_qk_norm_rope`` to ``ar_fp8_matmul``) take torch tensor
 only: types, sizes and strides come from them, and a tensor that does not fit
 raises ``ValueError`` before the call.  Without a ``stream`` they are enqueued, as
 torch's own operations are, on torch's current stream of the tensors' device.
+With one, torch's allocator does not know of the work there: a tensor made on
+another stream is kept until that work is done (or told with ``record_stream``).
 """
 from __future__ import annotations
 

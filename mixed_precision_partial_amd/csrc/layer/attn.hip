@@ -480,11 +480,11 @@ LAYER_DEV bool gathered_tile(const AttnArgs &a, int i, Seq &seq, int &tile) {
 // is done in half the time, which counts where a call has few of them.  Everyone of a
 // workgroup meets once for every S tiles of keys.
 // Bound by the matrix cores and the exponentials beside them: 8192 tokens, 32 heads over 8
-// of 128, causal, take 498 to 520 us, 1.06 PFLOP/s and more where a large bf16 product reaches 1.2; the matrix
-// cores are busy for 60 % of the cycles, and a score costs as many cycles of the
-// vector unit as of theirs.  Short calls are bound by the chain of a row's tiles (1.4 us each
+// of 128, causal, take 506 to 515 us, 1.07 PFLOP/s (the first calls after a rest 530 and
+// more), where a large bf16 product reaches 1.2; the matrix cores are busy for 60 % of the
+// cycles, and a score costs as many cycles of the vector unit as of theirs.  Short calls are bound by the chain of a row's tiles (1.4 us each
 // alone, about 1 with a second workgroup on the CU) and 5 us for beginning and end: 2048
-// tokens take 47 to 50 us.
+// tokens take 47 to 48 us.
 template <int T, int DB, int S>
 __global__ void __launch_bounds__(256 * S, DB <= 128 ? 2 / S : 1) k_attn_rows(AttnArgs a, unsigned tiles, bool gathered) {
     constexpr int KT = 64;

@@ -165,7 +165,8 @@ LAYER_DEV void fill_scales(float *da, float *db, const float *sa, const float *s
 
 // Tiles staged in LDS, two buffers: while one is multiplied the other is filled
 // straight from memory.  Bound by reading b where a has few rows (8192 x 8192 by 16, 67
-// MB: 14.3 us with the join of four splits, 4.7 TB/s); by the latency of a block's loads
+// MB: 14.3 us with the join of four splits, 4.7 TB/s, from the memory-side cache, and 20.4 with
+// a weight that was not just read); by the latency of a block's loads
 // where tiles are few (4001 columns by 333 rows, depth 2064: 16 us, 0.9 us a block); and by the
 // matrix cores otherwise (binary32 out, in bf16 products: 8192 x 8192 of depth 4096 in 519
 // us, 1.06 PFLOP/s, where a large bf16 product reaches 1.2).
@@ -441,7 +442,7 @@ LAYER_DEV void pin(v4f (&acc)[M][N]) {
 // products of those two fragments b's fragments of the next block are read, each into the
 // registers of the one just used up.  (2048 x 4096 of depth 4096, 128 x 128 tiles: 40 us so, 45
 // waiting for each block's loads before its products.)
-// 8192 cubed in 256 x 256 tiles: 477 to 507 us, 2.2 PFLOP/s (a library's product without block scales: 350 to 410 us).
+// 8192 cubed in 256 x 256 tiles: 470 to 515 us, 2.2 PFLOP/s (a library's product without block scales: 350 to 410 us).
 // The matrix cores are busy for 54 % of the cycles: a block's products take 2048 of a CU's
 // cycles, the additions of their results 1024 beside them, which two waves to a SIMD do not
 // wholly hide (2700 together); beginning and storing a tile costs as much as seven blocks.

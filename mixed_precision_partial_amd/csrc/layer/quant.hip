@@ -5,9 +5,10 @@
 //
 // A block belongs to 8 neighbouring lanes, 16 elements each: two 16-byte loads
 // (16-bit types), a maximum over 8 lanes, one 16-byte store.  Bound by bytes:
-// one read, one write of half of it.  On MI355X 8192 x 8192 in bf16 (203 MB) take 36.4
-// us, 5.6 TB/s: above the rate of a large copy (4.85), as a third of the traffic is
-// writes and not half; 32 x 4096 take 3 us, which is the launch.
+// one read, one write of half of it.  On MI355X 8192 x 8192 in bf16 (203 MB) take 36.4 to
+// 37.3 us, 5.5 TB/s: above the rate of a large copy (4.85), as a third of the traffic is
+// writes and not half; in binary32 (338 MB) 59.6 us, 5.7 TB/s; 32 x 4096 take 3 us, which is
+// the launch.
 #include <algorithm>
 
 #include "layer_device.h"

@@ -218,3 +218,23 @@ def test_attention_of_queries_past_32_bits(ctx, lens_q):
     want, wl, tol, tl = ref.attention(q, k, v, cu, ks, kl, True, 64 ** -0.5)
     base.near(out[:used], want[:used], tol[:used], "far queries")
     base.near(lse[:used], wl[:used], tl[:used], "their lse")
+
+
+# ------------------------------------------------------------------ codes by what they stand for
+
+@pytest.mark.parametrize("kind", [BF16, F16, F32], ids=str)
+def test_codes_stand_for_their_elements(ctx, kind):
+    """Scale times code against the element itself: half a step of e4m3, 2^-4 of the value, or of its
+    smallest ones, 2^-10; and the few binary32 roundings of the factor, the product and the scale."""
+    log_case(f"codes stand for their elements {kind}")
+    x = torch.randn(300, 1040, generator=base.gen(4)) * torch.logspace(-6, 4, 300, base=2.0)[:, None]
+    x[::7, 5::50] *= 100
+    x = x.to(kind)
+    out, scales = torch.empty(300, 1040, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(300, 9, device="cuda")
+    ar.ar_fp8_quantize(ctx, out, scales, x.cuda())
+    torch.cuda.synchronize()
+    s = scales.cpu().double().repeat_interleave(128, 1)[:, :1040]
+    top = torch.stack([x[:, c:c + 128].double().abs().amax(1) for c in range(0, 1040, 128)], 1) / 448
+    base.near(scales, top, ref.U32 * top, "scales")
+    want = x.double() / s
+    base.near(out.float(), want, 2.0 ** -4 * want.abs() + 2.0 ** -10 + 6 * ref.U32 * want.abs(), "codes")
