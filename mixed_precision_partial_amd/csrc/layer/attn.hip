@@ -771,6 +771,7 @@ __global__ void __launch_bounds__(64 * W, DB <= 128 ? 2 : 1) k_attn_keys(AttnArg
     auto values = [&](int t, const uint16_t *__restrict__ kg, char *__restrict__ kd, char *__restrict__ vc)
                       __attribute__((always_inline)) {
         if (t + W < t1) {
+            read_by_wave();                         // before the keys' buffer is filled again
             fill<DB, KT, 1, false>(kd, kg, a.k_token, (t + W) * KT, s.len_k, a.head_dim, 0);
             landed_but<DB / 16>();                  // the values; the next keys are under way
         } else {
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(64 * W, DB <= 128 ? 2 : 1) k_attn_keys(AttnArg
         tile_general<T, DB, KT>(kw, t * KT, free_to, a.scale_log2, w, p);
         values(t, kp, kw, vw);
         if (t + W < t1) {
-            read_by_wave();                         // before the buffer is filled again
+            read_by_wave();                         // before the values' is
             fill<DB, KT, 1, true>(vw, vp, a.v_token, (t + W) * KT, s.len_k, a.head_dim, 0);
         }
     }
